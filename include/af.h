@@ -353,7 +353,8 @@ af_status af_cache_read(const af_cache_config* cfg, const void* cache, int rows,
  * positions (clamped to 0..capacity) and n_q[b] queries (null: rows; clamped to
  * 0..rows), which are its last n_q[b] positions when causal != 0: query i
  * attends j <= length[b] - n_q[b] + i; when causal == 0, every live position.
- * A query that attends nothing gives zeros.  Rows n_q[b] .. rows-1 of a
+ * A query that attends nothing gives zeros; one that attends keys but has no
+ * finite score for any of them (a query row that is not finite) gives NaN.  Rows n_q[b] .. rows-1 of a
  * sequence are left as they were.  q, out: bf16 [batch, rows, heads *
  * head_dim]; length, n_q: int32 device arrays [batch].  scale > 0, finite.
  * rows * heads / kv_heads is at most 2^20.  Sums, softmax statistics and the

@@ -1,0 +1,81 @@
+"""Attention over the 4-bit cache at the edges of its arithmetic, whichever kernel a call goes to."""
+import math
+
+import pytest
+import torch
+
+from tests import ops_util as U
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def flow():
+    from video_generation_b200 import build
+    build.build()
+    from video_generation_b200 import flow as F
+    assert torch.cuda.is_available()
+    return F
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def exact_rows(cache, q, length, causal):
+    """ops_util.attention64 on the device, all rows of a sequence and head at once: (out, tolerance)."""
+    B, R, H, D = q.shape
+    k, v = (torch.from_numpy(x).cuda() for x in U.cache_values(cache.storage, B, cache.kv_heads, D, cache.capacity))
+    out, tol = torch.zeros(B, R, H, D, dtype=torch.float64, device="cuda"), torch.zeros(B, R, H, D, dtype=torch.float64, device="cuda")
+    scale = D ** -0.5
+    for b, L in enumerate(length):
+        for h in range(H):
+            x, K, V = q[b, :, h].double(), k[b, h // (H // cache.kv_heads), :L], v[b, h // (H // cache.kv_heads), :L]
+            s = x @ K.T * scale
+            if causal:
+                s.masked_fill_(torch.arange(L, device="cuda") > torch.arange(L - R, L, device="cuda")[:, None], -math.inf)
+            w = torch.softmax(s, 1)
+            d = scale * (U.HALF_BF16 * (x.abs() @ K.abs().T) +
+                         64 * U.HALF_FP32 * (x.abs() @ (K.abs() + 5 * K.abs().amax(1, keepdim=True)).T))
+            e = 2 * torch.expm1(2 * d) + 2 * U.HALF_BF16
+            out[b, :, h] = w @ V
+            tol[b, :, h] = (U.HALF_BF16 + (w * e).sum(1, keepdim=True)) * out[b, :, h].abs() + (w * e) @ V.abs() + 1e-30
+    return out, tol
+
+
+# ------------------------------------------------------------------ rows without a finite score
+
+def _signed_keys(B, cap, H, D, sign, seed):
+    g = torch.Generator().manual_seed(seed)
+    k = torch.randn(B, cap, H, D, generator=g)
+    k[..., 5] = sign * (1 + k[..., 5].abs())
+    return k.bfloat16().cuda(), torch.randn(B, cap, H, D, generator=g).bfloat16().cuda()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,cap", [(1, 60), (1, 3000), (9, 3000), (40, 9000), (100, 9000), (300, 700), (300, 9000)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_row_whose_scores_are_all_minus_infinity_is_nan(flow, D, rows, cap, causal):
+    """softmax of scores that are all -inf is NaN, not the zeros of a row that attends nothing: an infinite query
+    channel against keys of one sign, in the first row (few keys) and the last.  The other rows are what they are
+    without it, within their roundings (not bit for bit: next to a row with a NaN the tensor core's sums are rounded a
+    little differently)."""
+    B, H = 2, 2
+    for sign in (1.0, -1.0):
+        cache = flow.KVCache(B, H, D, cap)
+        flow.af_cache_write(cache, *_signed_keys(B, cap, H, D, sign, rows))
+        q = torch.randn(B, rows, H, D, generator=torch.Generator().manual_seed(7)).bfloat16().cuda()
+        want, tol = exact_rows(cache, q, [cap, rows], causal)
+        hit = torch.zeros(B, rows, H, dtype=torch.bool, device="cuda")
+        for r, value in ((0, math.inf), (0, -math.inf), (rows - 1, math.inf), (rows - 1, -math.inf)):
+            x = q.clone()
+            x[:, r, 1, 5] = value
+            got = flow.af_cache_attention(cache, x, ints([cap, rows]), causal=causal)
+            hit.zero_()
+            hit[:, r, 1] = True
+            assert torch.isnan(got[hit]).all()
+            assert ((got.double() - want).abs() <= tol)[~hit].all()
+        # with no key to attend it stays zero, whatever the row holds
+        x = q.clone()
+        x[:, :, :, 5] = -math.inf
+        assert (flow.af_cache_attention(cache, x, ints([0, 0]), causal=causal) == 0).all()

@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn4_tc(const Attn4Args a, int
         mx = mm;
       }
       const bool part = nsp > 1;
-      const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);   // a row that attends nothing is zero
+      const float inv = part ? 1.f : row_scale4(l, lim > 0);   // (without splits lim counts all its keys)
       // Rows go through the group's (now free) Q tile, HD bytes a row and warp at a time, so that the stores to
       // memory are contiguous: 16-byte unit x of row r at x ^ r.  All of the half row in bf16, or half of it in fp32.
       constexpr int U = HD / 16, RPI = 32 / U;

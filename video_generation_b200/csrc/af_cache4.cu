@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, HALF ? 4 : 3) k_attn4_small(
     }
     const int mr = m0 + r, i = mr / group, h = hk * group + mr - i * group;
     if (nsp == 1) {
-      const float inv = ls == 0.f ? 0.f : 1.f / ls;   // a row that attends nothing is zero
+      const float inv = row_scale4(ls, key_end4(a, sq, i) > 0);
       store4(a.o + sq.o0 + (size_t)i * a.o_rs + (size_t)h * D + c, v0 * inv, v1 * inv, v2 * inv, v3 * inv);
     } else {
       const size_t at = ((size_t)split * a.c.batch * a.c.kv_heads + bh) * mrows + mr;
@@ -776,8 +776,8 @@ __global__ void __launch_bounds__(128) k_attn4_combine(const Attn4Args a, int bk
       for (int k = 0; k < PER; ++k) acc[k] = s0 + u < nsp ? fmaf(x, v[u][k], acc[k]) : acc[k];
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
   const int i = mr / group, h = hk * group + mr - i * group;
+  const float inv = row_scale4(l, key_end4(a, sq, i) > 0);
   bf16* dst = a.o + sq.o0 + (size_t)i * a.o_rs + (size_t)h * D + PER * lane;
   if (PER == 4)
     store4(dst, acc[0] * inv, acc[1] * inv, acc[PER - 2] * inv, acc[PER - 1] * inv);

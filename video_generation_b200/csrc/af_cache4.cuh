@@ -152,6 +152,13 @@ __device__ __forceinline__ int key_end4(const Attn4Args& a, const Seq4& s, int i
   return a.causal ? max(0, min(s.len, s.len - s.nq + i + 1)) : s.len;
 }
 
+// 1 / l of a row's finished sum; a row that attends nothing gives zeros.  A row
+// with keys whose scores are all -inf (an infinite query channel against keys of
+// one sign there, or sums beyond fp32) has the sum 0 too, and is 0 / 0: NaN.
+__device__ __forceinline__ float row_scale4(float l, bool has_keys) {
+  return l != 0.f ? 1.f / l : (has_keys ? __int_as_float(0x7FC00000) : 0.f);
+}
+
 // Keys of one split of the tensor-core attention: the sequence's key tiles of
 // bkv keys in at most nsplit equal runs.
 __host__ __device__ __forceinline__ int tc_chunk4(int len, int nsplit, int bkv) {
