@@ -354,14 +354,16 @@ af_status af_cache_read(const af_cache_config* cfg, const void* cache, int rows,
  * 0..rows), which are its last n_q[b] positions when causal != 0: query i
  * attends j <= length[b] - n_q[b] + i; when causal == 0, every live position.
  * A query that attends nothing gives zeros; one that attends keys but has no
- * finite score for any of them (a query row that is not finite) gives NaN.  Rows n_q[b] .. rows-1 of a
- * sequence are left as they were.  q, out: bf16 [batch, rows, heads *
- * head_dim]; length, n_q: int32 device arrays [batch].  scale > 0, finite.
+ * finite score for any of them (a query row that is not finite) gives NaN.
+ * Rows n_q[b] .. rows-1 of a sequence are left as they were.  q, out: bf16
+ * [batch, rows, heads * head_dim]; length, n_q: int32 device arrays [batch].
+ * scale > 0, finite.
  * rows * heads / kv_heads is at most 2^20.  Sums, softmax statistics and the
  * output are fp32, rounded once; what enters the products is rounded once more
  * at most: weights and values to bf16, and, by the number of query rows, keys
- * to bf16 or queries to 14 bits of their row's largest value.  out must not
- * overlap q.  ws: af_cache_attention_workspace_bytes(cfg, heads, rows) bytes (the
+ * to bf16, or queries to 16 bits of their row's largest value (24 bits where a
+ * group of 32 channels would lose more than 2^-12 of its values by that).  out
+ * must not overlap q.  ws: af_cache_attention_workspace_bytes(cfg, heads, rows) bytes (the
  * current device decides; fewer rows can need more, since more splits of the
  * keys then share the work), 256-byte aligned, not shared by calls that may
  * overlap; it needs no initialisation and holds nothing between calls. */

@@ -1,6 +1,7 @@
 """Attention over the 4-bit cache at the edges of its arithmetic, whichever kernel a call goes to."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -79,3 +80,58 @@ def test_a_row_whose_scores_are_all_minus_infinity_is_nan(flow, D, rows, cap, ca
         x = q.clone()
         x[:, :, :, 5] = -math.inf
         assert (flow.af_cache_attention(cache, x, ints([0, 0]), causal=causal) == 0).all()
+
+
+# ------------------------------------------------------------------ queries with channels far above the others
+
+def _grid_rows(n, D, seed, silent):
+    """Key rows [n, D] that the cache holds exactly: multiples of 1/4 in -2 .. 7/4, both ends in every group of 32, and
+    0 (a code in the middle of the grid) in the `silent` channels."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randint(0, 16, (n, D // 32, 32), generator=g)
+    ends = torch.stack([torch.randperm(31, generator=g)[:2] + 1 for _ in range(n * D // 32)]).view(n, D // 32, 2)
+    x.scatter_(2, ends, torch.tensor([0, 15]).expand(n, D // 32, 2))
+    x = (x.flatten(1) - 8) / 4
+    x[:, silent] = 0
+    return x
+
+
+# (the silent channels are the first of their groups, which never hold a group's ends)
+@pytest.mark.parametrize("size", [1.0, 100.0, 1000.0, 30000.0])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,cap", [(1, 2000), (5, 700), (8, 333), (13, 2000), (16, 130), (40, 700), (200, 1300)])
+def test_a_channel_far_above_the_others(flow, D, rows, cap, size):
+    """The keys say nothing in the channel, so what it costs is what the others lose beside it.  Keys are exact here; the
+    output, the weights and the values are rounded to bf16, independently, each with an rms of 2^-8 / sqrt(3) at most:
+    0.004 of the output together, and the bound of the other attention tests, 0.006, holds whatever the channel's size."""
+    k = _grid_rows(cap, D, rows, [0, D - 32])[None, :, None].bfloat16()
+    v = torch.randn(1, cap, 1, D, generator=torch.Generator().manual_seed(3)).bfloat16()
+    q = torch.randn(1, rows, 1, D, generator=torch.Generator().manual_seed(4))
+    q[..., 0] = size
+    q[:, ::2, :, D - 32] = -size
+    q = q.bfloat16().cuda()
+    cache = flow.KVCache(1, 1, D, cap)
+    flow.af_cache_write(cache, k.cuda(), v.cuda())
+    K, V = U.cache_values(cache.storage, 1, 1, D, cap)
+    np.testing.assert_array_equal(K[0, 0], k[0, :, 0].double().numpy())
+    ref, tol = U.attention64(q, K, V, [cap], None, True, D ** -0.5)
+    got = flow.af_cache_attention(cache, q, ints([cap])).double().cpu().numpy()
+    err = np.abs(got - ref)
+    assert (err <= tol).all()
+    assert np.linalg.norm(err) <= 6e-3 * np.linalg.norm(ref), np.linalg.norm(err) / np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_query_does_not_depend_on_the_rows_beside_it(flow, D):
+    """One query alone (few-row kernel) and as the last of many (tensor cores): both within the roundings of the other."""
+    cap, rows = 4000, 300
+    g = torch.Generator().manual_seed(8)
+    cache = flow.KVCache(1, 2, D, cap)
+    flow.af_cache_write(cache, _grid_rows(2 * cap, D, 5, [0]).view(1, cap, 2, D).bfloat16().cuda(),
+                        torch.randn(1, cap, 2, D, generator=g).bfloat16().cuda())
+    q = torch.randn(1, rows, 2, D, generator=g)
+    q[..., 0] = 700.0
+    q = q.bfloat16().cuda()
+    many = flow.af_cache_attention(cache, q, ints([cap]))[:, -1:].double()
+    one = flow.af_cache_attention(cache, q[:, -1:].contiguous(), ints([cap])).double()
+    assert (many - one).norm() <= 2 * 6e-3 * many.norm()

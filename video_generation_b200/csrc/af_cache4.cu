@@ -1,5 +1,7 @@
 // af_cache4.cu -- the 4-bit key/value cache: writing rows, reading them back,
 // and attention of few query rows over it (layout: af_cache4.cuh).
+#include <type_traits>
+
 #include "af_cache4.cuh"
 #include "af_kernels.h"
 
@@ -240,14 +242,18 @@ __global__ void __launch_bounds__(256, 8) k_cache4_read(const Cache4R a) {
 // more instructions than anything else: the kernel is bound by issue, DRAM is
 // next.  Hence
 //   scores: the products run on the codes themselves, as bytes (three
-//     instructions for eight codes), in whole numbers: q is rounded to 14 bits
-//     of its row's largest value, q = d (64 a + b), a and b bytes in rows gr and
-//     gr + 8 of the 16-row operand, one product a group of 32 channels.  The
-//     group's step multiplies the exact sum:
+//     instructions for eight codes), in whole numbers: q = d (256 a + b), a and b
+//     bytes in rows gr and gr + 8 of the 16-row operand, one product a group of 32
+//     channels.  The group's step multiplies the exact sum:
 //     S = d sum_g s_g I_g + sum_g lo_g sum(q_g).
 //     The second sum is one more product with the parameters as operand and
-//     the sums of q split into two bf16 parts (a relative 2^-17).  The rounding
-//     of q is 2^-14 of its largest value, below what P's rounding does.
+//     the sums of q split into three bf16 parts (all 24 bits of them).
+//     d is a power of two that puts the row's largest value just below 2^15, so
+//     a bf16 value within 2^-7 of it is exact; with ordinary rows hardly any is
+//     not.  A channel far above the others leaves them fewer bits: where the
+//     rounding takes more than 2^-13 of a group's values (each counted up to
+//     2^11 d, so that the large ones do not hide the small), the CTA adds a
+//     third byte, q = d (256 a + b + c / 256), in one more product a group.
 //   values: v = lo + n s in packed bf16 (one rounding, 2^-8 relative at most),
 //     keys in pairs; they are the 16-row operand (channels) of O^T += V^T P^T, P
 //     the 8-column one, which halves the products for 8 rows;
@@ -273,11 +279,11 @@ __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uin
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// c = A B
-__device__ __forceinline__ void mma16808(float* c, uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+// c = A B with 16 of K, whose second 8 rows of B are its first 8 again
+__device__ __forceinline__ void mma16816_twice(float* c, const uint32_t* a, uint32_t b) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%8}, {%9,%9,%9,%9};"
                : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-               : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b), "f"(0.f));
 }
 // 8-bit whole numbers: A signed, B unsigned, 32 of K.  c = A B
 __device__ __forceinline__ void imma16832(int* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -395,9 +401,11 @@ __global__ void __launch_bounds__(kSmallWarps * 32, HALF ? 4 : 3) k_attn4_small(
   fetch();                                         // the first block travels while Q is made ready
 
   // Q, one group of channels a warp, handed round through shared memory: the
-  // bytes of 64 a + b of the group's channels 8 t + {0,4,1,5} and {2,6,3,7}
-  // for rows gr (and gr + 8), the row's factor d and the sums over each group.
+  // bytes of 256 a + b + c / 256 of the group's channels 8 t + {0,4,1,5} and
+  // {2,6,3,7} for rows gr (and gr + 8), the row's factor d and the sums over each
+  // group.
   __shared__ uint4 s_q[NQ][G][32];
+  __shared__ uint32_t s_qc[G][32][4];              // the bytes c: rows gr in words 0 and 2, rows gr + 8 in 1 and 3
   __shared__ float s_big[G][16], s_sum[G][16];
   int lim[2];                                      // keys that rows gr and gr + 8 of the tile attend
   int low = 0x7FFFFFFF;                            // the fewest keys that a row in use attends
@@ -439,42 +447,63 @@ __global__ void __launch_bounds__(kSmallWarps * 32, HALF ? 4 : 3) k_attn4_small(
   }
   __syncthreads();
   float qd[NQ];                                    // d
-  uint32_t qs[2] = {0u, 0u};                       // the sums of q as an A operand
+  uint32_t qs[4] = {0u, 0u, 0u, 0u};               // the sums of q as an A operand
+  bool lossy = false;                              // two bytes are too few for a row's group
 #pragma unroll
   for (int x = 0; x < NQ; ++x) {
-    float big = 1e-34f;                            // (a row of zeros, or of almost nothing)
+    float big = 1e-31f;                            // (a row of zeros, or of almost nothing)
 #pragma unroll
     for (int g = 0; g < G; ++g) big = fmaxf(big, s_big[g][gr + 8 * x]);
     const bool fin = big < INFINITY;
-    qd[x] = fin ? big * (1.f / 8128.f) : __int_as_float(0x7FC00000);   // a row that is not finite scores NaN
-    const float per = fin ? 8128.f / big : 0.f;
+    // exponent of d: big / d < 2^15, and at most 2^15 - 2^8, whose high byte is 127
+    const uint32_t bits = __float_as_uint(big) + 0x10000u, e = (bits >> 23) - 14;
+    qd[x] = fin ? __uint_as_float(e << 23) : __int_as_float(0x7FC00000);   // a row that is not finite scores NaN
     if (warp < G) {
+      const float per = __uint_as_float((254 - e) << 23) * 256.f;
       constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
-      uint32_t w[4] = {0u, 0u, 0u, 0u};            // a and b of four channels each, twice
+      uint32_t w[4] = {0u, 0u, 0u, 0u}, wc[2] = {0u, 0u};   // a and b of four channels each, twice; c likewise
+      int lost = 0, kept = 0;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int n = fin ? (int)rintf(f[x][order[4 * j + k]] * per) : 0;
-          const int top = (n + 32) >> 6;
+          const int m = (n + 128) >> 8, c = n - 256 * m, top = (m + 128) >> 8;
           w[2 * j] |= (uint32_t)(top & 255) << (8 * k);
-          w[2 * j + 1] |= (uint32_t)((n - 64 * top) & 255) << (8 * k);
+          w[2 * j + 1] |= (uint32_t)((m - 256 * top) & 255) << (8 * k);
+          wc[j] |= (uint32_t)(c & 255) << (8 * k);
+          lost += abs(c);
+          kept += min(abs(n), 1 << 19);
         }
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) {           // a row's group is in four lanes: at most 2^12 and 2^24
+        lost += __shfl_xor_sync(0xffffffffu, lost, o);
+        kept += __shfl_xor_sync(0xffffffffu, kept, o);
+      }
+      lossy = lossy || (lost << 13) > kept;
       s_q[x][warp][lane] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        s_qc[warp][lane][2 * j + x] = wc[j];
+        if (HALF) s_qc[warp][lane][2 * j + 1] = 0u;
+      }
     }
-    // k index 0-3 high part, 4-7 low part of the sum of group k & 3; lane t holds k = 2t, 2t + 1
-    float p[2] = {0.f, 0.f};
+    // k index 0-3 high part, 4-7 middle part, 8-11 low part of the sum of group k & 3, 12-15 nothing; lane t holds
+    // k = 2t, 2t + 1 and 2t + 8, 2t + 9
+    float p[2] = {0.f, 0.f}, p2[2] = {0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int g = 2 * (t & 1) + e;
       if (g < G) {
-        const float sum = s_sum[g][gr + 8 * x], hi = __bfloat162float(__float2bfloat16_rn(sum));
-        p[e] = t < 2 ? hi : sum - hi;
+        const float sum = s_sum[g][gr + 8 * x], hi = __bfloat162float(__float2bfloat16_rn(sum)), rest = sum - hi;
+        p[e] = t < 2 ? hi : rest;
+        p2[e] = t < 2 ? rest - __bfloat162float(__float2bfloat16_rn(rest)) : 0.f;
       }
     }
     qs[x] = pack2(p[0], p[1]);
+    qs[2 + x] = pack2(p2[0], p2[1]);
   }
-  __syncthreads();
+  lossy = __syncthreads_or(lossy);
   uint32_t qa[NQ][G][4];
 #pragma unroll
   for (int x = 0; x < NQ; ++x)
@@ -501,157 +530,178 @@ __global__ void __launch_bounds__(kSmallWarps * 32, HALF ? 4 : 3) k_attn4_small(
 
   int key0 = kbeg + kBlock * warp;
   constexpr int H = kBlock / 8;                    // tiles of 8 keys
+  // With and without the bytes c: one loop with a branch for them took 35.2 instead of 33.4 us where they are not
+  // needed (one row over 46800 keys of 16 heads of 128 channels; with them 40).
+  auto walk = [&](auto with_c) {
 #pragma unroll 1
-  for (int n = 0; n < my_blocks; ++n, key0 += (int)ADV) {
-    fetch();
-    cp_wait<1>();
-    __syncwarp();
-    const uint8_t* st = ring + (n & 1) * Cfg::STAGE;
-    // ---- scores of the block: keys 8 h + .. in the columns of tile h
-    float s[H][2 * NQ];
+    for (int n = 0; n < my_blocks; ++n, key0 += (int)ADV) {
+      fetch();
+      cp_wait<1>();
+      __syncwarp();
+      const uint8_t* st = ring + (n & 1) * Cfg::STAGE;
+      // ---- scores of the block: keys 8 h + .. in the columns of tile h
+      float s[H][2 * NQ];
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      uint32_t w[G], pa[G], pb[G];                 // codes of key 8 h + gr; parameters of keys 8 h + 2 t, + 1
-      const uint8_t* par = st + Cfg::CODES + (8 * h + 2 * t) * (D / 8);
-      uint2 own;                                   // parameters of key 8 h + gr (operand of the offset product)
-      if (D == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(st + h * 512 + okc);
-        const uint4 y = *reinterpret_cast<const uint4*>(par), z = *reinterpret_cast<const uint4*>(par + 16);
-        w[0] = x.x; w[1] = x.y; w[G - 2] = x.z; w[G - 1] = x.w;
-        pa[0] = y.x; pa[1] = y.y; pa[G - 2] = y.z; pa[G - 1] = y.w;
-        pb[0] = z.x; pb[1] = z.y; pb[G - 2] = z.z; pb[G - 1] = z.w;
-        own = *reinterpret_cast<const uint2*>(st + Cfg::CODES + (8 * h + gr) * 16 + (t & 1) * 8);
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(st + h * 256 + okc);
-        const uint4 y = *reinterpret_cast<const uint4*>(par);
-        w[0] = x.x; w[1] = x.y;
-        pa[0] = y.x; pa[1] = y.y;
-        pb[0] = y.z; pb[1] = y.w;
-        own = *reinterpret_cast<const uint2*>(st + Cfg::CODES + (8 * h + gr) * 8);
-      }
-      float off[4];                                // sum_g lo_g sum(q_g)
-      mma16808(off, qs[0], qs[1], __byte_perm(own.x, own.y, 0x7632));
-      float acc[2 * NQ];
-#pragma unroll
-      for (int x = 0; x < 2 * NQ; ++x) acc[x] = 0.f;
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const uint32_t k0 = w[g] & 0x0F0F0F0Fu, k1 = (w[g] >> 4) & 0x0F0F0F0Fu;
-        const float sa = __uint_as_float(pa[g] << 16), sb = __uint_as_float(pb[g] << 16);
-#pragma unroll
-        for (int x = 0; x < NQ; ++x) {
-          int c[4];
-          imma16832(c, qa[x][g][0], qa[x][g][1], qa[x][g][2], qa[x][g][3], k0, k1);
-          acc[2 * x] = fmaf(sa, (float)(c[0] * 64 + c[2]), acc[2 * x]);   // below 2^22: exact
-          acc[2 * x + 1] = fmaf(sb, (float)(c[1] * 64 + c[3]), acc[2 * x + 1]);
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < 2 * NQ; ++x) s[h][x] = fmaf(qd[x >> 1], acc[x], off[x]);
-    }
-    // ---- softmax: this lane's keys key0 + 8 h + 2 t + {0, 1}
-    if (key0 + kBlock > low) {
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-#pragma unroll
-        for (int e = 0; e < 2 * NQ; ++e)
-          if (key0 + 8 * h + 2 * t + (e & 1) >= lim[e >> 1]) s[h][e] = -INFINITY;
-    }
-    uint32_t p[NQ][H];
-    float add[NQ];
-    auto exponentials = [&]() {
-#pragma unroll
-      for (int x = 0; x < NQ; ++x) {
-        const float nm = mx[x] == -INFINITY ? 0.f : -mx[x];
-        add[x] = 0.f;
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          const float e0 = ex2(fmaf(s[h][2 * x], a.scale_log2, nm)), e1 = ex2(fmaf(s[h][2 * x + 1], a.scale_log2, nm));
-          add[x] += e0 + e1;
-          p[x][h] = pack2(e0, e1);
-        }
-      }
-    };
-    exponentials();
-    bool raise = (mx[0] == -INFINITY && lim[0] > 0) || add[0] > kMost;
-    if (!HALF) raise = raise || (mx[1] == -INFINITY && lim[1] > 0) || add[NQ - 1] > kMost;
-    if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-      for (int x = 0; x < NQ; ++x) {
-        float m = fmaxf(s[0][2 * x], s[0][2 * x + 1]), f = 1.f;
-#pragma unroll
-        for (int h = 1; h < H; ++h) m = fmaxf(m, fmaxf(s[h][2 * x], s[h][2 * x + 1]));
-        m *= a.scale_log2;
-#pragma unroll
-        for (int d = 1; d <= 2; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        m = fmaxf(m, mx[x]);
-        if (mx[x] != -INFINITY) f = ex2(mx[x] - m);
-        mx[x] = m;
-        l[x] *= f;
-        // the factors of this lane's columns of O^T
-        const float fa = __shfl_sync(0xffffffffu, f, 8 * t), fb = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-#pragma unroll
-        for (int i = 0; i < G * 2; ++i) {
-          o[x][i][0] *= fa;
-          o[x][i][1] *= fb;
-          o[x][i][2] *= fa;
-          o[x][i][3] *= fb;
-        }
-      }
-      exponentials();
-    }
-#pragma unroll
-    for (int x = 0; x < NQ; ++x) l[x] += add[x];
-    // ---- O^T += V^T P^T, 16 keys at a time: keys 2t, 2t+1 and 2t+8, 2t+9 of this lane, channel parity gr & 1 of
-    // unit gr / 2
-    const uint8_t* sv = st + Cfg::CODES + Cfg::PARS;
-#pragma unroll
-    for (int j = 0; j < H / 2; ++j) {
-      uint32_t vw[2][G], ps[2][G], pl[2][G];       // code pairs, (s, s) and (lo, lo) of the two keys
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int h = 2 * j + e;
-        const uint8_t* vpar = sv + Cfg::CODES + (8 * h + 2 * t) * (D / 8);
-        uint32_t xa[G], xb[G], ya[G], yb[G];       // codes and parameters of the two keys
+      for (int h = 0; h < H; ++h) {
+        uint32_t w[G], pa[G], pb[G];                 // codes of key 8 h + gr; parameters of keys 8 h + 2 t, + 1
+        const uint8_t* par = st + Cfg::CODES + (8 * h + 2 * t) * (D / 8);
+        uint2 own;                                   // parameters of key 8 h + gr (operand of the offset product)
         if (D == 128) {
-          const uint4 c0 = *reinterpret_cast<const uint4*>(sv + h * 512 + ovc), c1 = *reinterpret_cast<const uint4*>(sv + h * 512 + ovc + 64);
-          const uint4 d0 = *reinterpret_cast<const uint4*>(vpar), d1 = *reinterpret_cast<const uint4*>(vpar + 16);
-          xa[0] = c0.x; xa[1] = c0.y; xa[G - 2] = c0.z; xa[G - 1] = c0.w;
-          xb[0] = c1.x; xb[1] = c1.y; xb[G - 2] = c1.z; xb[G - 1] = c1.w;
-          ya[0] = d0.x; ya[1] = d0.y; ya[G - 2] = d0.z; ya[G - 1] = d0.w;
-          yb[0] = d1.x; yb[1] = d1.y; yb[G - 2] = d1.z; yb[G - 1] = d1.w;
+          const uint4 x = *reinterpret_cast<const uint4*>(st + h * 512 + okc);
+          const uint4 y = *reinterpret_cast<const uint4*>(par), z = *reinterpret_cast<const uint4*>(par + 16);
+          w[0] = x.x; w[1] = x.y; w[G - 2] = x.z; w[G - 1] = x.w;
+          pa[0] = y.x; pa[1] = y.y; pa[G - 2] = y.z; pa[G - 1] = y.w;
+          pb[0] = z.x; pb[1] = z.y; pb[G - 2] = z.z; pb[G - 1] = z.w;
+          own = *reinterpret_cast<const uint2*>(st + Cfg::CODES + (8 * h + gr) * 16 + (t & 1) * 8);
         } else {
-          const uint2 c0 = *reinterpret_cast<const uint2*>(sv + h * 256 + ovc), c1 = *reinterpret_cast<const uint2*>(sv + h * 256 + ovc + 32);
-          const uint4 d = *reinterpret_cast<const uint4*>(vpar);
-          xa[0] = c0.x; xa[1] = c0.y;
-          xb[0] = c1.x; xb[1] = c1.y;
-          ya[0] = d.x; ya[1] = d.y;
-          yb[0] = d.z; yb[1] = d.w;
+          const uint2 x = *reinterpret_cast<const uint2*>(st + h * 256 + okc);
+          const uint4 y = *reinterpret_cast<const uint4*>(par);
+          w[0] = x.x; w[1] = x.y;
+          pa[0] = y.x; pa[1] = y.y;
+          pb[0] = y.z; pb[1] = y.w;
+          own = *reinterpret_cast<const uint2*>(st + Cfg::CODES + (8 * h + gr) * 8);
         }
+        float off[4];                                // sum_g lo_g sum(q_g)
+        mma16816_twice(off, qs, __byte_perm(own.x, own.y, 0x7632));
+        float acc[2 * NQ];
+#pragma unroll
+        for (int x = 0; x < 2 * NQ; ++x) acc[x] = 0.f;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          vw[e][g] = __byte_perm(xa[g], xb[g], sel);
-          ps[e][g] = __byte_perm(ya[g], yb[g], 0x5410);
-          pl[e][g] = __byte_perm(ya[g], yb[g], 0x7632);
+          const uint32_t k0 = w[g] & 0x0F0F0F0Fu, k1 = (w[g] >> 4) & 0x0F0F0F0Fu;
+          const float sa = __uint_as_float(pa[g] << 16), sb = __uint_as_float(pb[g] << 16);
+#pragma unroll
+          for (int x = 0; x < NQ; ++x) {
+            int c[4];
+            imma16832(c, qa[x][g][0], qa[x][g][1], qa[x][g][2], qa[x][g][3], k0, k1);
+            acc[2 * x] = fmaf(sa, (float)(c[0] * 256 + c[2]), acc[2 * x]);   // below 2^24: exact
+            acc[2 * x + 1] = fmaf(sb, (float)(c[1] * 256 + c[3]), acc[2 * x + 1]);
+          }
         }
+        if constexpr (decltype(with_c)::value) {     // the bytes c of both sets of rows in one product
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const uint4 v = *reinterpret_cast<const uint4*>(s_qc[g][lane]);
+            int c[4];
+            imma16832(c, v.x, v.y, v.z, v.w, w[g] & 0x0F0F0F0Fu, (w[g] >> 4) & 0x0F0F0F0Fu);
+            const float sa = __uint_as_float(pa[g] << 16) * (1.f / 256.f), sb = __uint_as_float(pb[g] << 16) * (1.f / 256.f);
+#pragma unroll
+            for (int x = 0; x < 2 * NQ; ++x) acc[x] = fmaf(x & 1 ? sb : sa, (float)c[x], acc[x]);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2 * NQ; ++x) s[h][x] = fmaf(qd[x >> 1], acc[x], off[x]);
+      }
+      // ---- softmax: this lane's keys key0 + 8 h + 2 t + {0, 1}
+      if (key0 + kBlock > low) {
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int e = 0; e < 2 * NQ; ++e)
+            if (key0 + 8 * h + 2 * t + (e & 1) >= lim[e >> 1]) s[h][e] = -INFINITY;
+      }
+      uint32_t p[NQ][H];
+      float add[NQ];
+      auto exponentials = [&]() {
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+          const float nm = mx[x] == -INFINITY ? 0.f : -mx[x];
+          add[x] = 0.f;
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            const float e0 = ex2(fmaf(s[h][2 * x], a.scale_log2, nm)), e1 = ex2(fmaf(s[h][2 * x + 1], a.scale_log2, nm));
+            add[x] += e0 + e1;
+            p[x][h] = pack2(e0, e1);
+          }
+        }
+      };
+      exponentials();
+      bool raise = (mx[0] == -INFINITY && lim[0] > 0) || add[0] > kMost;
+      if (!HALF) raise = raise || (mx[1] == -INFINITY && lim[1] > 0) || add[NQ - 1] > kMost;
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+          float m = fmaxf(s[0][2 * x], s[0][2 * x + 1]), f = 1.f;
+#pragma unroll
+          for (int h = 1; h < H; ++h) m = fmaxf(m, fmaxf(s[h][2 * x], s[h][2 * x + 1]));
+          m *= a.scale_log2;
+#pragma unroll
+          for (int d = 1; d <= 2; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+          m = fmaxf(m, mx[x]);
+          if (mx[x] != -INFINITY) f = ex2(mx[x] - m);
+          mx[x] = m;
+          l[x] *= f;
+          // the factors of this lane's columns of O^T
+          const float fa = __shfl_sync(0xffffffffu, f, 8 * t), fb = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+#pragma unroll
+          for (int i = 0; i < G * 2; ++i) {
+            o[x][i][0] *= fa;
+            o[x][i][1] *= fb;
+            o[x][i][2] *= fa;
+            o[x][i][3] *= fb;
+          }
+        }
+        exponentials();
       }
 #pragma unroll
-      for (int g = 0; g < G; ++g)
+      for (int x = 0; x < NQ; ++x) l[x] += add[x];
+      // ---- O^T += V^T P^T, 16 keys at a time: keys 2t, 2t+1 and 2t+8, 2t+9 of this lane, channel parity gr & 1 of
+      // unit gr / 2
+      const uint8_t* sv = st + Cfg::CODES + Cfg::PARS;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t v[2][2];                        // [key half][channel row gr or gr + 8]
+      for (int j = 0; j < H / 2; ++j) {
+        uint32_t vw[2][G], ps[2][G], pl[2][G];       // code pairs, (s, s) and (lo, lo) of the two keys
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < 2; ++e) {
+          const int h = 2 * j + e;
+          const uint8_t* vpar = sv + Cfg::CODES + (8 * h + 2 * t) * (D / 8);
+          uint32_t xa[G], xb[G], ya[G], yb[G];       // codes and parameters of the two keys
+          if (D == 128) {
+            const uint4 c0 = *reinterpret_cast<const uint4*>(sv + h * 512 + ovc);
+            const uint4 c1 = *reinterpret_cast<const uint4*>(sv + h * 512 + ovc + 64);
+            const uint4 d0 = *reinterpret_cast<const uint4*>(vpar), d1 = *reinterpret_cast<const uint4*>(vpar + 16);
+            xa[0] = c0.x; xa[1] = c0.y; xa[G - 2] = c0.z; xa[G - 1] = c0.w;
+            xb[0] = c1.x; xb[1] = c1.y; xb[G - 2] = c1.z; xb[G - 1] = c1.w;
+            ya[0] = d0.x; ya[1] = d0.y; ya[G - 2] = d0.z; ya[G - 1] = d0.w;
+            yb[0] = d1.x; yb[1] = d1.y; yb[G - 2] = d1.z; yb[G - 1] = d1.w;
+          } else {
+            const uint2 c0 = *reinterpret_cast<const uint2*>(sv + h * 256 + ovc);
+            const uint2 c1 = *reinterpret_cast<const uint2*>(sv + h * 256 + ovc + 32);
+            const uint4 d = *reinterpret_cast<const uint4*>(vpar);
+            xa[0] = c0.x; xa[1] = c0.y;
+            xb[0] = c1.x; xb[1] = c1.y;
+            ya[0] = d.x; ya[1] = d.y;
+            yb[0] = d.z; yb[1] = d.w;
+          }
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              v[e][k] = dequant2(lop_and_or(vw[e][g] >> (8 * i + 4 * k), 0x000F000Fu, 0x43004300u), ps[e][g], pl[e][g]);
-#pragma unroll
-          for (int x = 0; x < NQ; ++x)
-            mma16816(o[x][2 * g + i], v[0][0], v[0][1], v[1][0], v[1][1], p[x][2 * j], p[x][2 * j + 1]);
+          for (int g = 0; g < G; ++g) {
+            vw[e][g] = __byte_perm(xa[g], xb[g], sel);
+            ps[e][g] = __byte_perm(ya[g], yb[g], 0x5410);
+            pl[e][g] = __byte_perm(ya[g], yb[g], 0x7632);
+          }
         }
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t v[2][2];                        // [key half][channel row gr or gr + 8]
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                v[e][k] = dequant2(lop_and_or(vw[e][g] >> (8 * i + 4 * k), 0x000F000Fu, 0x43004300u), ps[e][g], pl[e][g]);
+#pragma unroll
+            for (int x = 0; x < NQ; ++x)
+              mma16816(o[x][2 * g + i], v[0][0], v[0][1], v[1][0], v[1][1], p[x][2 * j], p[x][2 * j + 1]);
+          }
+      }
+      __syncwarp();                                  // the stage may be written again
     }
-    __syncwarp();                                  // the stage may be written again
-  }
+  };
+  if (lossy)
+    walk(std::true_type{});
+  else
+    walk(std::false_type{});
   cp_wait<0>();
 #pragma unroll
   for (int x = 0; x < NQ; ++x)
