@@ -178,8 +178,9 @@ af_status af_prefix_encode(const af_model* m, const float* x, int batch, int L, 
  * flow-encoded into the cache (af_prefix_encode); the rest are generated by
  * block-Jacobi (tau, max_iter, warm_start as in af_inverse_jacobi).
  * iters [batch, n_frames] holds each frame's count from the window that
- * generated it.  ws: af_stream_workspace_bytes(m, batch, window) (a
- * window's workspace plus staging of its x and z).  0 <= overlap < window. */
+ * generated it.  ws: af_stream_workspace_bytes(m, batch, window) (the most
+ * that a window of up to `window` frames needs, plus staging of its x and z).
+ * 0 <= overlap < window. */
 size_t af_stream_workspace_bytes(const af_model* m, int batch, int window);
 af_status af_inverse_jacobi_stream(const af_model* m, const float* z, int batch, int n_frames, int window, int overlap,
                                    float tau, int max_iter, int warm_start, float* x, int32_t* iters, void* ws,
@@ -187,7 +188,8 @@ af_status af_inverse_jacobi_stream(const af_model* m, const float* z, int batch,
 
 /* Bytes of the shallow-side workspace of flow_pipeline_inverse for T shallow
  * blocks (config of `shallow`), `batch` videos, frames of frame_len tokens,
- * `group` frames per shallow call; 0 on a bad argument. */
+ * up to `group` frames per shallow call (a shorter last group can need more
+ * than a full one); 0 on a bad argument. */
 size_t flow_pipeline_workspace_bytes(const af_model* shallow, int T, int batch, int frame_len, int group);
 
 /* Pipelined deep -> shallow decoding ("Key design 3": the deep flow

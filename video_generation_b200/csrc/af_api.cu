@@ -8,6 +8,7 @@
 // design 3 (block-wise Jacobi with KV cache, warm start and the tau test).
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -1075,13 +1076,49 @@ af_status af_prefix_encode(const af_model* m, const float* x, int batch, int L, 
   return graph_run(m, key, (cudaStream_t)stream, build_encode, &c);
 }
 
-size_t flow_pipeline_workspace_bytes(const af_model* shallow, int T, int batch, int frame_len, int group) {
-  if (!shallow || T < 1 || batch < 1 || group < 1) return 0;
-  const int nb = batch * group;                    // a shallow call's samples: group frames of every video
-  const size_t stack = af_workspace_bytes(shallow, nb, frame_len, frame_len);
+}  // extern "C"
+
+namespace {
+
+// Workspace of the calls that flow_pipeline_inverse makes on groups of 1 ..
+// `group` frames of every video, and af_inverse_jacobi_stream on windows of 1 ..
+// `window` frames.  The largest call need not need the most: with fewer rows
+// the keys and the residual GEMMs are split more ways.  0 on a bad argument.
+size_t group_ws(const af_model* shallow, int batch, int frame_len, int group) {
+  size_t most = 0;
+  if ((int64_t)batch * group * frame_len > INT_MAX) return 0;   // rows are counted in 32 bits
+  for (int g = 1; g <= group; ++g) {
+    const size_t n = af_workspace_bytes(shallow, batch * g, frame_len, frame_len);
+    if (!n) return 0;
+    most = n > most ? n : most;
+  }
+  return most;
+}
+// With the frames on their way in and out, and their counts (samples: group
+// frames of every video).
+size_t pipeline_ws(size_t stack, const af_model* shallow, int T, int batch, int frame_len, int group) {
   if (!stack) return 0;
-  const size_t frames = align256((size_t)nb * frame_len * shallow->cfg.C * sizeof(float));
-  return stack + 2 * frames + align256((size_t)T * nb * sizeof(int32_t));
+  const int nb = batch * group;
+  return stack + 2 * align256((size_t)nb * frame_len * shallow->cfg.C * sizeof(float)) +
+         align256((size_t)T * nb * sizeof(int32_t));
+}
+size_t window_ws(const af_model* m, int batch, int window) {
+  size_t most = 0;
+  for (int n = 1; n <= window; ++n) {
+    const size_t b = af_workspace_bytes(m, batch, n * m->cfg.frame_len, m->cfg.frame_len);
+    if (!b) return 0;
+    most = b > most ? b : most;
+  }
+  return most;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t flow_pipeline_workspace_bytes(const af_model* shallow, int T, int batch, int frame_len, int group) {
+  if (!shallow || T < 1 || batch < 1 || group < 1 || frame_len < 1) return 0;
+  return pipeline_ws(group_ws(shallow, batch, frame_len, group), shallow, T, batch, frame_len, group);
 }
 
 af_status flow_pipeline_inverse(const af_model* deep, const af_model* const* shallow, const af_dir* shallow_dirs, int T,
@@ -1109,7 +1146,9 @@ af_status flow_pipeline_inverse(const af_model* deep, const af_model* const* sha
   const int nf = L / F;
   if (group < 1 || group > nf) { set_err("need 1 <= group <= L / frame_len (%d), got %d", nf, group); return AF_ERR_ARG; }
   if (af_status s = check_ws(deep, ws_deep, ws_deep_bytes, batch, L, B)) return s;
-  const size_t need_s = flow_pipeline_workspace_bytes(shallow[0], T, batch, F, group);
+  const size_t stack_bytes = group_ws(shallow[0], batch, F, group);
+  const size_t need_s = pipeline_ws(stack_bytes, shallow[0], T, batch, F, group);
+  if (!need_s) { set_err("too many frames in a shallow call"); return AF_ERR_ARG; }
   if (!ws_shallow || (reinterpret_cast<uintptr_t>(ws_shallow) & 255u) || ws_shallow_bytes < need_s) {
     set_err("shallow workspace: need %zu bytes, 256-aligned; got %zu", need_s, ws_shallow_bytes);
     return AF_ERR_WORKSPACE;
@@ -1119,10 +1158,9 @@ af_status flow_pipeline_inverse(const af_model* deep, const af_model* const* sha
     CK(cudaEventCreateWithFlags(&dm->ev_frame, cudaEventDisableTiming));
     CK(cudaEventCreateWithFlags(&dm->ev_done, cudaEventDisableTiming));
   }
-  // the shallow side's workspace: the stack's own (for batch * group samples),
-  // then the staged frames in / out and the counts
+  // the shallow side's workspace: the stack's own, then the staged frames in /
+  // out and the counts
   const int nbmax = batch * group;
-  const size_t stack_bytes = af_workspace_bytes(shallow[0], nbmax, F, F);
   const size_t frames = align256((size_t)nbmax * F * C * sizeof(float));
   char* wsS = static_cast<char*>(ws_shallow);
   float* stage_in = (float*)(wsS + stack_bytes);
@@ -1168,7 +1206,7 @@ size_t af_stream_workspace_bytes(const af_model* m, int batch, int window) {
   if (!m || batch < 1 || window < 1) return 0;
   const int F = m->cfg.frame_len;
   const int Lw = window * F;
-  const size_t base = af_workspace_bytes(m, batch, Lw, F);
+  const size_t base = window_ws(m, batch, window);
   if (!base) return 0;
   const size_t frames = align256((size_t)batch * Lw * m->cfg.C * sizeof(float));
   return base + 2 * frames + align256((size_t)batch * window * sizeof(int32_t));
@@ -1194,8 +1232,8 @@ af_status af_inverse_jacobi_stream(const af_model* m, const float* z, int batch,
     return AF_ERR_WORKSPACE;
   }
   // the window's own workspace, then the staged window of x and z and its counts
-  const size_t win_bytes = af_workspace_bytes(m, batch, window * F, F);
   const size_t frames = align256((size_t)batch * window * F * C * sizeof(float));
+  const size_t win_bytes = need - 2 * frames - align256((size_t)batch * window * sizeof(int32_t));
   char* base = static_cast<char*>(ws);
   float* xw = (float*)(base + win_bytes);
   float* zw = (float*)(base + win_bytes + frames);
