@@ -1172,33 +1172,41 @@ af_status flow_pipeline_inverse(const af_model* deep, const af_model* const* sha
   Schedule sc = uniform_schedule(L, B);
   const size_t frame_bytes = (size_t)F * C * sizeof(float);
   const size_t video_pitch = (size_t)L * C * sizeof(float);
-  for (int f = 0; f < nf; ++f) {
-    // f_D^{-1}: the blocks of frame f (the table once, then only the range)
-    sc.b_begin = f * bpf;
-    sc.b_end = (f + 1) * bpf;
-    if (f > 0) launch_set_range(carve(deep, ws_deep, batch, L, B).btab, sc.b_begin, sc.b_end, sd);
-    if (af_status s = run_inverse(dblk, ddir, 1, z, batch, L, sc, tau, max_iter_deep, warm_start, u, iters_deep,
-                                  ws_deep, sd, f == 0))
-      return s;
-    const int f0 = (f / group) * group;           // first frame of f's group
-    const int g = (f0 + group <= nf ? group : nf - f0);
-    if (f != f0 + g - 1) continue;                // the group is not complete yet
-    CK(cudaEventRecord(dm->ev_frame, sd));
-    // f_S^{-1} of frames f0 .. f on the second stream, while f_D goes on:
-    // every video's g frames, each frame a sample of its own ([batch * g, F, C])
-    CK(cudaStreamWaitEvent(ss, dm->ev_frame, 0));
-    const size_t run = (size_t)g * frame_bytes;
-    CK(cudaMemcpy2DAsync(stage_in, run, u + (size_t)f0 * F * C, video_pitch, run, batch, cudaMemcpyDeviceToDevice, ss));
-    if (af_status s = flow_stack_inverse(shallow, shallow_dirs, T, stage_in, batch * g, F, F, tau, max_iter_shallow, 0,
-                                         stage_out, stage_it, ws_shallow, stack_bytes, ss))
-      return s;
-    CK(cudaMemcpy2DAsync(x + (size_t)f0 * F * C, video_pitch, stage_out, run, run, batch, cudaMemcpyDeviceToDevice, ss));
-    // counts [T, batch * g] -> iters_shallow[T, batch, f0 .. f0 + g)
-    CK(cudaMemcpy2DAsync(iters_shallow + f0, (size_t)nf * sizeof(int32_t), stage_it, (size_t)g * sizeof(int32_t),
-                         (size_t)g * sizeof(int32_t), (size_t)T * batch, cudaMemcpyDeviceToDevice, ss));
-  }
-  CK(cudaEventRecord(dm->ev_done, ss));
-  CK(cudaStreamWaitEvent(sd, dm->ev_done, 0));
+  auto enqueue = [&]() -> af_status {
+    for (int f = 0; f < nf; ++f) {
+      // f_D^{-1}: the blocks of frame f (the table once, then only the range)
+      sc.b_begin = f * bpf;
+      sc.b_end = (f + 1) * bpf;
+      if (f > 0) launch_set_range(carve(deep, ws_deep, batch, L, B).btab, sc.b_begin, sc.b_end, sd);
+      if (af_status s = run_inverse(dblk, ddir, 1, z, batch, L, sc, tau, max_iter_deep, warm_start, u, iters_deep,
+                                    ws_deep, sd, f == 0))
+        return s;
+      const int f0 = (f / group) * group;           // first frame of f's group
+      const int g = (f0 + group <= nf ? group : nf - f0);
+      if (f != f0 + g - 1) continue;                // the group is not complete yet
+      CK(cudaEventRecord(dm->ev_frame, sd));
+      // f_S^{-1} of frames f0 .. f on the second stream, while f_D goes on:
+      // every video's g frames, each frame a sample of its own ([batch * g, F, C])
+      CK(cudaStreamWaitEvent(ss, dm->ev_frame, 0));
+      const size_t run = (size_t)g * frame_bytes;
+      CK(cudaMemcpy2DAsync(stage_in, run, u + (size_t)f0 * F * C, video_pitch, run, batch, cudaMemcpyDeviceToDevice, ss));
+      if (af_status s = flow_stack_inverse(shallow, shallow_dirs, T, stage_in, batch * g, F, F, tau, max_iter_shallow, 0,
+                                           stage_out, stage_it, ws_shallow, stack_bytes, ss))
+        return s;
+      CK(cudaMemcpy2DAsync(x + (size_t)f0 * F * C, video_pitch, stage_out, run, run, batch, cudaMemcpyDeviceToDevice, ss));
+      // counts [T, batch * g] -> iters_shallow[T, batch, f0 .. f0 + g)
+      CK(cudaMemcpy2DAsync(iters_shallow + f0, (size_t)nf * sizeof(int32_t), stage_it, (size_t)g * sizeof(int32_t),
+                           (size_t)g * sizeof(int32_t), (size_t)T * batch, cudaMemcpyDeviceToDevice, ss));
+    }
+    return AF_OK;
+  };
+  const af_status s = enqueue();
+  // stream_deep waits for the shallow side after an error too: what was
+  // enqueued before it still uses the caller's buffers
+  const cudaError_t e = cudaEventRecord(dm->ev_done, ss), w = cudaStreamWaitEvent(sd, dm->ev_done, 0);
+  if (s) return s;
+  CK(e);
+  CK(w);
   return AF_OK;
 }
 
