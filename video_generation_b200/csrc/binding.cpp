@@ -7,12 +7,14 @@
 // The functions check shapes, types, strides and devices, make outputs that
 // are not given, and call the library.  They return the outputs, or the
 // library's status as an int when it is not AF_OK; a tensor that cannot be
-// passed on raises ValueError.
+// passed on raises ValueError.  None of the calls has a gradient: a tensor that
+// autograd follows is refused, and what a call writes moves its version counter.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/EmptyTensor.h>
 #include <c10/core/Allocator.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
@@ -38,7 +40,14 @@ struct PyFailed {};   // a Python error is set already
 const at::Tensor* tensor(const char* what, PyObject* o, bool optional) {
   if (o == Py_None && optional) return nullptr;
   if (!THPVariable_Check(o)) bad(std::string(what) + ": not a tensor");
-  return &THPVariable_Unpack(o);
+  const at::Tensor* t = &THPVariable_Unpack(o);
+  if (c10::GradMode::is_enabled() && t->requires_grad())
+    bad(std::string(what) + ": a tensor that requires grad, and the call has no gradient: make it under torch.no_grad(), or of detached tensors");
+  return t;
+}
+// The caller's tensor was written behind autograd's back: a graph that saved it must not use it.
+void written(const at::Tensor* t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
 }
 void on_device(const char* what, const at::Tensor* t, int dev) {
   if (t && (!t->is_cuda() || t->get_device() != dev))
@@ -177,6 +186,8 @@ PyObject* qk_norm_rope(PyObject* const* a, Py_ssize_t n) {
                             static_cast<const float*>(at_(qg)), static_cast<const float*>(at_(kg)), p, at_(out[0]), os[0],
                             at_(out[1]), os[1], stream_of(dev));
   if (st) return status(st);
+  written(q ? qo : nullptr);
+  written(k ? ko : nullptr);
   PyObject* r = PyTuple_New(2);
   if (!r) throw PyFailed{};
   for (int i = 0; i < 2; ++i) {
@@ -215,6 +226,7 @@ PyObject* cache_write(PyObject* const* a, Py_ssize_t n) {
   const af_status st = p_write(c, store->data_ptr(), (int)k->size(1), k->data_ptr(), batch_stride(*k, ks), ks,
                                v->data_ptr(), batch_stride(*v, vs), vs, s, m, stream_of(dev));
   if (st) return status(st);
+  written(store);
   Py_RETURN_NONE;
 }
 
@@ -246,6 +258,10 @@ PyObject* cache_read(PyObject* const* a, Py_ssize_t n) {
   const af_status st = p_read(c, store->data_ptr(), (int)rows, s, m, dtype_of(type), k->data_ptr(), v->data_ptr(),
                               batch_stride(*k, ks), ks, stream_of(dev));
   if (st) return status(st);
+  if (!made[0].defined()) {
+    written(k);
+    written(v);
+  }
   PyObject* r = PyTuple_New(2);
   if (!r) throw PyFailed{};
   for (int i = 0; i < 2; ++i) {
@@ -300,6 +316,7 @@ PyObject* cache_attention(PyObject* const* a, Py_ssize_t n) {
                               causal != 0, (float)scale, out->data_ptr(), batch_stride(*out, os), os, ws->data_ptr(),
                               (size_t)ws->nbytes(), stream_of(dev));
   if (st) return status(st);
+  if (!made.defined()) written(out);
   if (made.defined()) {
     PyObject* o = THPVariable_Wrap(made);
     if (!o) throw PyFailed{};

@@ -359,6 +359,7 @@ def af_inverse_jacobi_stream(model: AFModel, z: torch.Tensor, window: int, overl
 
 
 # ---- operators of one attention layer (no model) ----
+# For inference: none has a gradient, and a tensor that requires grad is refused unless gradients are off.
 
 ROPE_PAIRS, ROPE_HALVES = 0, 1
 
