@@ -52,3 +52,27 @@ def test_it_is_taken_where_gradients_are_off(flow, cache):
                 with pytest.raises((ValueError, RuntimeError)) as e:
                     call()
                 assert "requires grad" not in str(e.value)
+
+
+def test_a_workspace_that_is_not_dense_is_refused(flow, cache):
+    """A broadcast byte says that it has as many as it is asked for."""
+    x = rows(2, 3, 2, 64)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 24), torch.zeros(1 << 16, 2, dtype=torch.uint8)[:, 0]):
+        with pytest.raises(ValueError, match="contiguous"):
+            flow.af_cache_attention(cache, x, ints(3, 3), ws=ws)
+
+
+@pytest.mark.parametrize("bad", [lambda n: torch.zeros(n - 1, dtype=torch.uint8),
+                                 lambda n: torch.zeros(1, dtype=torch.uint8).expand(n),
+                                 lambda n: torch.zeros(n, 2, dtype=torch.uint8)[:, 1]])
+def test_a_storage_that_changed_after_the_handle_was_made_is_refused(flow, cache, bad):
+    x = rows(2, 3, 2, 64)
+    cache.storage = bad(cache.bytes)
+    for call in (lambda: flow.af_cache_write(cache, x, x), lambda: flow.af_cache_read(cache, 3),
+                 lambda: flow.af_cache_read(cache, 3, k=x, v=x.clone()), lambda: flow.af_cache_attention(cache, x, ints(3, 3))):
+        with pytest.raises(ValueError, match="contiguous|needs"):
+            call()
+    cache.storage = torch.zeros(cache.bytes, dtype=torch.uint8)
+    cache.storage.resize_(cache.bytes // 2)
+    with pytest.raises(ValueError, match="needs"):
+        flow.af_cache_write(cache, x, x)

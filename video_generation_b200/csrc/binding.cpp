@@ -32,6 +32,7 @@ decltype(&::af_cache_write) p_write;
 decltype(&::af_cache_read) p_read;
 decltype(&::af_cache_attention) p_attn;
 decltype(&::af_cache_attention_workspace_bytes) p_ws;
+decltype(&::af_cache_bytes) p_bytes;
 
 // What ends a call as a Python ValueError.
 [[noreturn]] void bad(const std::string& msg) { throw std::invalid_argument(msg); }
@@ -84,6 +85,17 @@ const int32_t* ints(const char* what, const at::Tensor* t, int64_t n, int64_t m 
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type) {
   return at::detail::empty_generic(shape, c10::GetAllocator(at::kCUDA), c10::DispatchKeySet(c10::DispatchKey::CUDA), type,
                                    std::nullopt);
+}
+// A buffer that a call addresses by the byte: nothing but a dense one has the
+// memory that its size says (a broadcast one has less).
+void dense(const char* what, const at::Tensor* t) {
+  if (t && !t->is_contiguous()) bad(std::string(what) + ": not contiguous");
+}
+// The cache's storage, which is checked when the handle is made but may have been replaced or resized since.
+void storage(const char* what, const at::Tensor* t, const af_cache_config* c) {
+  dense(what, t);
+  if (t->nbytes() < p_bytes(c))
+    bad(std::string(what) + ": the cache needs " + std::to_string(p_bytes(c)) + " bytes, its storage has " + std::to_string(t->nbytes()));
 }
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(dev).stream(); }
 bool good_type(at::ScalarType t) { return t == at::kBFloat16 || t == at::kFloat; }
@@ -140,6 +152,7 @@ PyObject* load(PyObject* const* a, Py_ssize_t n) {
   p_read = (decltype(p_read))sym("af_cache_read");
   p_attn = (decltype(p_attn))sym("af_cache_attention");
   p_ws = (decltype(p_ws))sym("af_cache_attention_workspace_bytes");
+  p_bytes = (decltype(p_bytes))sym("af_cache_bytes");
   p_qk = (decltype(p_qk))sym("af_qk_norm_rope");
   Py_RETURN_NONE;
 }
@@ -214,6 +227,7 @@ PyObject* cache_write(PyObject* const* a, Py_ssize_t n) {
   const af_cache_config* c = address<const af_cache_config>(a[0]);
   const at::Tensor *store = tensor(what, a[1], false), *k = tensor(what, a[2], false), *v = tensor(what, a[3], false),
                    *start = tensor(what, a[4], true), *count = tensor(what, a[5], true);
+  storage("af_cache_write: storage", store, c);
   if (k->dim() != 4 || v->sizes() != k->sizes() || k->size(0) != c->batch)
     bad("af_cache_write: k and v are [" + std::to_string(c->batch) + ", rows, " + std::to_string(c->kv_heads) + ", " +
         std::to_string(c->head_dim) + "], got " + shape_of(*k) + " and " + shape_of(*v));
@@ -241,6 +255,7 @@ PyObject* cache_read(PyObject* const* a, Py_ssize_t n) {
   const long rows = number(a[2]);
   const at::ScalarType type = number(a[5]) ? at::kFloat : at::kBFloat16;
   if (rows < 0 || rows > INT_MAX || !k != !v) bad("af_cache_read: rows >= 0, and k and v both given or neither");
+  storage("af_cache_read: storage", store, c);
   const int dev = c10::cuda::current_device();
   at::Tensor made[2];
   if (!k) {
@@ -288,6 +303,8 @@ PyObject* cache_attention(PyObject* const* a, Py_ssize_t n) {
   const af_cache_config* c = address<const af_cache_config>(a[0]);
   const at::Tensor *store = tensor(what, a[1], false), *q = tensor(what, a[2], false), *length = tensor(what, a[3], false),
                    *nq = tensor(what, a[4], true), *ws = tensor(what, a[7], true), *out = tensor(what, a[8], true);
+  storage("af_cache_attention: storage", store, c);
+  dense("af_cache_attention: ws", ws);
   if (q->dim() != 4 || q->size(0) != c->batch)
     bad("af_cache_attention: q is [" + std::to_string(c->batch) + ", rows, heads, " + std::to_string(c->head_dim) +
         "], got " + shape_of(*q));
