@@ -55,3 +55,22 @@ def test_calls_in_inference_mode_and_without_gradients(flow):
         assert torch.equal(flow.af_cache_attention(c, y, length, out=out), want)
     flow.af_cache_write(c, x, x)                             # an inference tensor, written outside
     assert torch.equal(flow.af_cache_attention(c, x, length), want)
+
+
+def test_outputs_whose_strides_differ_where_they_say_nothing(flow):
+    """One sequence and one row: rows of unlike buffers have one layout."""
+    cache = flow.KVCache(1, 2, 64, 8)
+    x = torch.randn(1, 4, 2, 64, device="cuda").bfloat16()
+    flow.af_cache_write(cache, x, x)
+    start = torch.tensor([2], dtype=torch.int32, device="cuda")
+    want, _ = flow.af_cache_read(cache, 1, start=start)
+    wide = torch.zeros(5, 7, 3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    k, v = wide[1:2, 3:4, 1], torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    assert k.stride() != v.stride()
+    flow.af_cache_read(cache, 1, start=start, k=k, v=v)
+    assert torch.equal(k, want) and torch.equal(v, want) and int((wide != 0).sum()) == int((want != 0).sum())
+    # rows that do differ stay refused
+    for k, v in ((wide[:1, :4, 0], torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16, device="cuda")),
+                 (wide[:1, :4, 0], wide[:1, 3:6, 0].flatten(2).unflatten(2, (2, 64)).contiguous())):
+        with pytest.raises(ValueError):
+            flow.af_cache_read(cache, 4, k=k, v=v)

@@ -265,11 +265,15 @@ PyObject* cache_read(PyObject* const* a, Py_ssize_t n) {
   }
   for (const at::Tensor* t : {store, k, v, start, count}) on_device(what, t, dev);
   const int32_t *s = ints("af_cache_read: start", start, c->batch), *m = ints("af_cache_read: count", count, c->batch);
-  if (k->dim() != 4 || k->size(0) != c->batch || k->size(1) != rows || v->sizes() != k->sizes() || v->strides() != k->strides())
+  auto unlike = [&] {
     bad("af_cache_read: k and v are [" + std::to_string(c->batch) + ", " + std::to_string(rows) + ", " +
         std::to_string(c->kv_heads) + ", " + std::to_string(c->head_dim) + "] of one layout");
+  };
+  if (k->dim() != 4 || k->size(0) != c->batch || k->size(1) != rows || v->sizes() != k->sizes()) unlike();
   const int64_t ks = row_stride("af_cache_read: k", *k, c->kv_heads, c->head_dim, type);
-  row_stride("af_cache_read: v", *v, c->kv_heads, c->head_dim, type);
+  // (strides of dimensions of one element say nothing)
+  const int64_t vs = row_stride("af_cache_read: v", *v, c->kv_heads, c->head_dim, type);
+  if (vs != ks || batch_stride(*v, vs) != batch_stride(*k, ks)) unlike();
   const af_status st = p_read(c, store->data_ptr(), (int)rows, s, m, dtype_of(type), k->data_ptr(), v->data_ptr(),
                               batch_stride(*k, ks), ks, stream_of(dev));
   if (st) return status(st);
