@@ -359,7 +359,7 @@ af_status af_cache_read(const af_cache_config* cfg, const void* cache, int rows,
  * finite score for any of them (a query row that is not finite) gives NaN.
  * Rows n_q[b] .. rows-1 of a sequence are left as they were.  q, out: bf16
  * [batch, rows, heads * head_dim]; length, n_q: int32 device arrays [batch].
- * scale > 0, finite.
+ * 0 < scale <= 2^127.
  * rows * heads / kv_heads is at most 2^20.  Sums, softmax statistics and the
  * output are fp32, rounded once; what enters the products is rounded once more
  * at most: weights and values to bf16, and, by the number of query rows, keys

@@ -118,3 +118,10 @@ def test_nothing_to_do_needs_no_device(flow):
         assert L.af_cache_write(cfg, P, rows, None, 0, 0, None, 0, 0, None, None, None) == 0
         assert L.af_cache_read(cfg, P, rows, None, None, 1, None, None, 0, 0, None) == 0
         assert L.af_cache_attention(cfg, P, rows, 2, None, 0, 0, None, None, 1, 0.1, None, 0, 0, None, 0, None) == 0
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 3.4e38])
+def test_a_scale_whose_log2_units_are_not_finite_is_refused(flow, scale):
+    """scale * log2(e) is what multiplies the scores: infinite, it would make NaN of a score of 0."""
+    _rejected(flow, flow.lib().af_cache_attention(_cfg(flow), P, 3, 4, P, 768, 256, P, None, 1, scale, 2 * P, 768, 256, P,
+                                                  1 << 20, None))

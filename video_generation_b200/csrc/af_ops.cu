@@ -262,7 +262,8 @@ af_status af_cache_attention(const af_cache_config* cfg, const void* cache, int 
   if (af_status s = check_cache(what, cfg, cache)) return s;
   if (!good_heads(cfg, heads, rows))
     return bad("%s: need heads a multiple of kv_heads, and 0 <= rows * heads / kv_heads <= 2^20", what);
-  if (!(scale > 0.f) || !isfinite(scale)) return bad("%s: scale must be positive and finite", what);
+  const float scale_log2 = (float)(scale * 1.4426950408889634);   // scores in units of log2
+  if (!(scale > 0.f) || !isfinite(scale_log2)) return bad("%s: scale must be positive and at most 2^127", what);
   if (rows == 0 || cfg->batch == 0) return AF_OK;
   const int64_t n = (int64_t)heads * cfg->head_dim;
   if (!q || !aligned16(q) || !in_stride(q_row_stride, 2) || !in_stride(q_batch_stride, 2))
@@ -294,7 +295,7 @@ af_status af_cache_attention(const af_cache_config* cfg, const void* cache, int 
   a.causal = causal != 0;
   a.len = length;
   a.nq = n_q;
-  a.scale_log2 = (float)(scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   a.nsplit = p.nsplit;
   a.even = p.even;
   a.opart = (float*)((char*)ws + 256);
