@@ -48,11 +48,37 @@ def _stale(target: str, deps: list) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
+def _binding_lacks(torch) -> str | None:
+    """What this machine lacks for the binding, or None.  libaf.so needs none of it."""
+    if torch is None or not os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")):
+        return "PyTorch with CUDA"
+    if shutil.which("g++") is None:
+        return "g++"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    return None
+
+
 def _build_binding(cuda: str, force: bool, verbose: bool) -> None:
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    """Builds _binding.so; where that is impossible it is left out (the operators' Python calls then say so), and the
+    library still serves C callers and the other Python calls."""
+    torch = _torch_dir()
     src = os.path.join(CSRC, "binding.cpp")
-    if not force and not _stale(BINDING, [src, os.path.join(INCLUDE, "af.h"), os.path.join(torch, "version.py"),
-                                          os.path.abspath(__file__)]):
+    deps = [src, os.path.join(INCLUDE, "af.h"), os.path.abspath(__file__)]
+    if torch:
+        deps.append(os.path.join(torch, "version.py"))
+    if not force and not _stale(BINDING, deps):
+        return
+    lacks = _binding_lacks(torch)
+    if lacks:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)   # of other sources
+        sys.stderr.write(f"_binding.so not built: it needs {lacks}\n")
         return
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I" + os.path.join(torch, "include"),
            "-I" + os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-I" + os.path.join(cuda, "include"),
