@@ -167,7 +167,7 @@ Bufs carve(const af_model* m, void* ws, int batch, int L, int B) {
   b.nsplit = m->bf ? attn_tc_splits(batch, c.heads, rows_per_sample(L, B), L, m->num_sms) : 1;
   if (m->cache_bits == 4) {
     int even;
-    b.tc4 = attn4_use_tc(batch, c.heads, 1, rows_per_sample(L, B), L, m->hd);
+    b.tc4 = attn4_use_tc(batch, c.heads, 1, rows_per_sample(L, B), L, m->hd, m->num_sms);
     b.nsplit = b.tc4 ? attn4_tc_splits(batch, c.heads, 1, rows_per_sample(L, B), L, m->num_sms)
                      : attn4_small_splits(batch, c.heads, 1, rows_per_sample(L, B), L, m->num_sms, &even);
   }

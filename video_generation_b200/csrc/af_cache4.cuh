@@ -113,13 +113,13 @@ cudaError_t launch_attn4_small(const Attn4Args& a, cudaStream_t st);
 // heads do with four sequences (18 against 20 us) and do not with one (12 and 17);
 // 390 rows over 16 keys of 192 heads do (26 against 63 us).  Over 292 calls of 16 to
 // 800 keys and 48 to 4096 heads the rule loses 0.4% on average and 1.36 times at worst.
-inline bool attn4_use_tc(int batch, int kv_heads, int group, int rows, int cap, int head_dim) {
+inline bool attn4_use_tc(int batch, int kv_heads, int group, int rows, int cap, int head_dim, int num_sms) {
   const double m = (double)rows * group, heads = (double)batch * kv_heads;
   const double tiles = (double)(((long long)rows * group + 15) / 16), blocks = (double)(((long long)rows * group + 255) / 256);
   auto starts = [](double ctas, double fit, double us) { return ctas > 0.5 * fit ? us * (ctas / fit - 0.5) : 0.0; };
-  const double small = (head_dim == 128 ? 52e-6 : 30e-6) * tiles * heads * cap + starts(tiles * heads, 3 * 148, 5);
+  const double small = (head_dim == 128 ? 52e-6 : 30e-6) * tiles * heads * cap + starts(tiles * heads, 3.0 * num_sms, 5);
   const double each = head_dim == 128 ? (m <= 128 ? 105e-6 : 160e-6 * blocks) : (m <= 128 ? 87e-6 : 140e-6 * blocks);
-  return m > 16 && small - each * heads * cap - starts(blocks * heads, 148, 10) > 5;
+  return m > 16 && small - each * heads * cap - starts(blocks * heads, num_sms, 10) > 5;
 }
 // The tensor-core kernel (af_attn4_tc.cu) takes 128 or 256 packed rows a CTA;
 // err: the error word of its bounded waits (null: that of calls without a model).

@@ -126,7 +126,7 @@ struct AttnPlan {
 AttnPlan attn_plan(const af_cache_config* c, int heads, int rows, int sms) {
   AttnPlan p{};
   const int group = heads / c->kv_heads;
-  p.tc = attn4_use_tc(c->batch, c->kv_heads, group, rows, c->capacity, c->head_dim);
+  p.tc = attn4_use_tc(c->batch, c->kv_heads, group, rows, c->capacity, c->head_dim, sms);
   p.nsplit = p.tc ? attn4_tc_splits(c->batch, c->kv_heads, group, rows, c->capacity, sms)
                   : attn4_small_splits(c->batch, c->kv_heads, group, rows, c->capacity, sms, &p.even);
   if (p.nsplit > 1) {
