@@ -135,3 +135,30 @@ def test_a_query_does_not_depend_on_the_rows_beside_it(flow, D):
     many = flow.af_cache_attention(cache, q, ints([cap]))[:, -1:].double()
     one = flow.af_cache_attention(cache, q[:, -1:].contiguous(), ints([cap])).double()
     assert (many - one).norm() <= 2 * 6e-3 * many.norm()
+
+
+# ------------------------------------------------------------------ waits past the limit
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [100, 300])                # 128 rows a CTA and 256
+def test_a_wait_past_the_limit_is_given_up_and_reported(flow, D, rows):
+    """Calls long enough that some wait is not over when it is first looked at: with a limit of a nanosecond one gives up
+    (code 4), the CTAs drain (never code 2) and end, and the next call is as before."""
+    H, cap = 16, 46800
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cache = flow.KVCache(1, H, D, cap)
+    flow.af_cache_write(cache, *(torch.randn(1, cap, H, D, generator=g, device="cuda").bfloat16() for _ in range(2)))
+    q = torch.randn(1, rows, H, D, generator=g, device="cuda").bfloat16()
+    want = flow.af_cache_attention(cache, q, ints([cap]))
+    assert flow.operator_error() == 0
+    flow.operator_wait_limit(1e-9)
+    try:
+        codes = []
+        for _ in range(8):
+            flow.af_cache_attention(cache, q, ints([cap]))
+            codes.append(flow.operator_error())
+    finally:
+        flow.operator_wait_limit(2.0)
+    assert set(codes) <= {0, 4} and 4 in codes
+    assert torch.equal(flow.af_cache_attention(cache, q, ints([cap])), want)
+    assert flow.operator_error() == 0
