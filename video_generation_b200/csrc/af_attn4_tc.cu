@@ -44,8 +44,9 @@
 // 390 queries over 46800 keys 231 us (645; 122 of its two CTAs' 512 rows are no
 // one's).  No pipe is full (tensor 39%, exponentials 41%, ALU 46%): what bounds it
 // is issue, 63% of the cycles, of which about a quarter goes into waits, and the
-// chain S -> P -> O of each group.  Tiles of 128 keys, one thread a row, groups
-// in turn and alternating tiles all came to 300 to 340 us for the 8190 queries.
+// chain S -> P -> O of each group.  For the 8190 queries one score buffer of
+// 128 columns and one thread a row took 516 us, two buffers of 64 took 438, issue
+// by converged warps 428, two threads a row 299.
 //
 // Every wait is bounded; on expiry the CTA stops, waits for its copies and
 // MMAs in flight, frees TMEM and reports ERR_ATTN_WAIT.

@@ -264,10 +264,11 @@ __global__ void __launch_bounds__(256, 8) k_cache4_read(const Cache4R a) {
 // CTA attends are zero-filled on the way in, so nothing stored there is used.
 // P is rounded to bf16 for the product (its sum l stays fp32).
 //
-// Measured: one row over 46800 keys of 16 heads of 128 channels 33.6 us (120 MB,
-// 3.6 TB/s; the instructions issue in 61% of the cycles, the ALU pipe is half
-// taken), one row in 32 sequences of up to 8192 keys with 32 query and 8 key
-// heads 49 us, one row over 390 keys of 4 x 12 heads of 64 channels 4.5 us.
+// Measured: one row over 46800 keys of 16 heads of 128 channels 34 us (120 MB,
+// 3.5 TB/s; the instructions issue in 62% of the cycles, the ALU pipe is half
+// taken), 40 us with the third byte, one row in 32 sequences of up to 8192 keys
+// with 32 query and 8 key heads 51 us, one row over 390 keys of 4 x 12 heads of
+// 64 channels 4.4 us.
 constexpr int kSmallWarps = 4;
 constexpr int kSmallStages = 2;
 constexpr int kBlock = 32;        // keys of a warp's step
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, HALF ? 4 : 3) k_attn4_small(
   int key0 = kbeg + kBlock * warp;
   constexpr int H = kBlock / 8;                    // tiles of 8 keys
   // With and without the bytes c: one loop with a branch for them took 35.2 instead of 33.4 us where they are not
-  // needed (one row over 46800 keys of 16 heads of 128 channels; with them 40).
+  // needed (one row over 46800 keys of 16 heads of 128 channels; two loops with them 40).
   auto walk = [&](auto with_c) {
 #pragma unroll 1
     for (int n = 0; n < my_blocks; ++n, key0 += (int)ADV) {

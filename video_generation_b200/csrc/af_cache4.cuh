@@ -109,10 +109,12 @@ cudaError_t launch_attn4_small(const Attn4Args& a, cudaStream_t st);
 // more to start and finish.  With many CTAs their own starts add up: 5 us for each
 // three CTAs an SM of the small kernel, 10 us for each one of the other.
 // So with 128 channels 48 rows over 46800 keys of 16 heads go to the tensor cores
-// (76 against 104 us) and 24 rows do not (78 and 75); 96 rows over 2000 keys of 4
-// heads do with four sequences (18 against 20 us) and do not with one (12 and 17);
-// 390 rows over 16 keys of 192 heads do (26 against 63 us).  Over 292 calls of 16 to
-// 800 keys and 48 to 4096 heads the rule loses 0.4% on average and 1.36 times at worst.
+// (76 against 107 us) and 24 rows do not (74 against 80: the rule's error); 96 rows
+// over 2000 keys of 8 heads do with four sequences (21 against 30 us), over 4
+// heads with one they do not (18 against 13); 390 rows over 16 keys of 192 heads do
+// (26 against 66 us).  Both kernels timed on 148 SMs, over 292 calls of 16 to 800
+// keys and 48 to 4096 heads the rule loses 0.5% on average and 1.28 times at worst,
+// over 198 calls of 17 to 390 rows and 2000 to 46800 keys 0.8% and 1.19 times.
 inline bool attn4_use_tc(int batch, int kv_heads, int group, int rows, int cap, int head_dim, int num_sms) {
   const double m = (double)rows * group, heads = (double)batch * kv_heads;
   const double tiles = (double)(((long long)rows * group + 15) / 16), blocks = (double)(((long long)rows * group + 255) / 256);
