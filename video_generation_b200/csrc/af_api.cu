@@ -14,6 +14,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <atomic>
 #include <map>
 #include <string>
 #include <vector>
@@ -64,6 +65,13 @@ struct LayerW {
 
 }  // namespace
 
+// A number that no model of the process has had before: a model made where a
+// destroyed one lay must not be taken for it by a graph of another block.
+static long long next_version() {
+  static std::atomic<long long> last{0};
+  return ++last;
+}
+
 struct af_model {
   af_config cfg;
   int fd, hd;
@@ -85,7 +93,7 @@ struct af_model {
   int rot_width;
   float *q_gain, *k_gain;
   int cache_bits;     // 16: the KV cache holds activations; 4: quantised (af_set_cache_bits)
-  int version;        // counts the settings above: part of every graph's key
+  long long version;  // of the model and the settings above: part of every graph's key (next_version)
   int l2_keep;        // keep the hidden state / residual stream / attention output in L2 (evict_last stores)
   std::vector<void*> allocs;
   // graph cache (keyed by every pointer and scalar baked into the graph)
@@ -847,7 +855,7 @@ af_status create_model(const af_config* cfg, const float* const* tensors, int n_
   m->rot_width = 0;
   m->q_gain = m->k_gain = nullptr;
   m->cache_bits = 16;
-  m->version = 0;
+  m->version = next_version();
   m->l2_keep = 1;
   if (const char* v = getenv("AF_L2_KEEP")) m->l2_keep = atoi(v) != 0;
   if (const char* v = getenv("AF_PDL")) m->pdl = atoi(v) != 0;
@@ -1304,7 +1312,7 @@ af_status af_set_rotary(af_model* m, const af_rope* rope, int width, const float
   if (!m) { set_err("null model"); return AF_ERR_ARG; }
   if (!rope) {
     m->rot_width = 0;
-    ++m->version;
+    m->version = next_version();
     return AF_OK;
   }
   if (const char* why = af::rope_fault(rope)) { set_err("af_set_rotary: %s", why); return AF_ERR_ARG; }
@@ -1332,7 +1340,7 @@ af_status af_set_rotary(af_model* m, const af_rope* rope, int width, const float
   m->rot_width = width;
   m->q_gain = dev[0];
   m->k_gain = dev[1];
-  ++m->version;
+  m->version = next_version();
   return AF_OK;
 }
 
@@ -1343,7 +1351,7 @@ af_status af_set_cache_bits(af_model* m, int bits) {
     return AF_ERR_ARG;
   }
   m->cache_bits = bits;
-  ++m->version;
+  m->version = next_version();
   return AF_OK;
 }
 
