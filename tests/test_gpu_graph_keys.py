@@ -39,3 +39,22 @@ def test_a_model_made_after_another_was_destroyed(flow):
         assert torch.equal(z, want) and torch.allclose(ld, ld0 + ld1, rtol=1e-6, atol=1e-3)
         second.close()
     print("addresses used again:", len(handles) - len(set(handles)))
+
+
+def test_the_wait_limit_of_every_block_of_a_stack(flow):
+    """A limit set on the second block after the stack's graph was captured."""
+    first, second = _model(flow, 0), _model(flow, 1)
+    x = to_dev(syn.make_latents(2, 130, 64, 3))
+    ws, z, ld = first.workspace(2, 130), torch.empty_like(x), torch.empty(2, device="cuda")
+
+    def run():
+        flow.flow_stack_forward([first, second], [O.L2R, O.R2L], x, ws=ws, z=z, logdet=ld)
+        return first.device_error(), second.device_error()
+
+    assert run() == (0, 0)
+    want = z.clone()
+    second.set_wait_limit(1e-9)
+    codes = [run() for _ in range(3)]
+    assert all(a == 0 for a, _ in codes) and any(b for _, b in codes) and not any(b & 2 for _, b in codes)
+    second.set_wait_limit(2.0)
+    assert run() == (0, 0) and torch.equal(z, want)

@@ -693,8 +693,8 @@ af_status run_inverse(const af_model* const* blocks, const af_dir* dirs, int T, 
   uint32_t taubits;
   memcpy(&taubits, &tau, 4);
   std::string key = keyf("inv", {(long long)z, (long long)x, (long long)iters, (long long)ws, batch, L, sc.B_max, nb,
-                                 (long long)taubits, max_iter, c.warm, T, (long long)blocks[0]->wait_ns});
-  for (int t = 0; t < T; ++t) key += keyf("", {(long long)blocks[t], blocks[t]->version, dirs[t]});
+                                 (long long)taubits, max_iter, c.warm, T});
+  for (int t = 0; t < T; ++t) key += keyf("", {(long long)blocks[t], blocks[t]->version, (long long)blocks[t]->wait_ns, dirs[t]});
   return graph_run(blocks[0], key, st, build_inverse, &c);
 }
 
@@ -1007,10 +1007,9 @@ af_status flow_stack_forward(const af_model* const* blocks, const af_dir* dirs, 
   if (!x || !z || !logdet || x == z) { set_err("x/z/logdet (x and z must not alias)"); return AF_ERR_ARG; }
   if (af_status s = check_ws(blocks[0], ws, ws_bytes, batch, L, L)) return s;
   FwdCtx c{blocks, dirs, T, batch, L, x, z, logdet, carve(blocks[0], ws, batch, L, L)};
-  std::vector<long long> kv = {(long long)x, (long long)z, (long long)logdet, (long long)ws, batch, L, T,
-                               (long long)blocks[0]->wait_ns};
+  std::vector<long long> kv = {(long long)x, (long long)z, (long long)logdet, (long long)ws, batch, L, T};
   std::string key = keyf("fwd", {});
-  for (int t = 0; t < T; ++t) key += keyf("", {(long long)blocks[t], blocks[t]->version, dirs[t]});
+  for (int t = 0; t < T; ++t) key += keyf("", {(long long)blocks[t], blocks[t]->version, (long long)blocks[t]->wait_ns, dirs[t]});
   for (long long v : kv) key += keyf("", {v});
   return graph_run(blocks[0], key, (cudaStream_t)stream, build_forward, &c);
 }
