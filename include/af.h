@@ -364,7 +364,7 @@ af_status af_cache_read(const af_cache_config* cfg, const void* cache, int rows,
  * output are fp32, rounded once; what enters the products is rounded once more
  * at most: weights and values to bf16, and, by the number of query rows, keys
  * to bf16, or queries to 16 bits of their row's largest value (24 bits where a
- * group of 32 channels would lose more than 2^-12 of its values by that).  out
+ * group of 32 channels would lose more than 2^-13 of its values by that).  out
  * must not overlap q.  ws: af_cache_attention_workspace_bytes(cfg, heads, rows) bytes (the
  * current device decides; fewer rows can need more, since more splits of the
  * keys then share the work), 256-byte aligned, not shared by calls that may
